@@ -568,7 +568,9 @@ nvfp4_status nvfp4_kv_cache_read(const nvfp4_kv_cache* cache, int64_t tokens, co
  * over a paged cache.
  *
  * Scores and sums are FP32; the probabilities enter the second product as FP16
- * with a 2^7 scale (relative step 2^-11).
+ * with a 2^7 scale (relative step 2^-11, down to 2^-21 of the row's largest),
+ * with NVFP4_KV_SCALE_TOKEN times their token's scale as two bf16 parts (2^-17):
+ * what a token adds keeps its precision whatever the other tokens' scales are.
  *
  * q, out       : device, bf16 [batch][heads][head_dim] with the given batch and
  *                head strides in elements; q rows on 16-byte boundaries

@@ -12,15 +12,19 @@
 // register i of lane group g is token 4g + i of its 16-token tile, and two tiles make the 32 tokens of
 // one second product, in that order.  V's bytes take the same order by loading each lane group's own
 // eight tokens (a run of head_dim/16 bytes of each) and transposing 4 x 4 bytes in registers.
-// K's codes widen to bf16 and V's to FP16, both exactly; the queries stay bf16.  The probabilities are
-// rounded to FP16, scaled by 2^7: a relative step of 2^-11 down to 2^-21 of the row's largest, below
-// the bf16 output's own 2^-8.
+// K's codes widen to bf16, exactly; the queries stay bf16.  With a scale per tensor or head V's codes widen to FP16,
+// exactly too, and the probabilities are rounded to FP16, scaled by 2^7: a relative step of 2^-11 down to 2^-21 of the
+// row's largest, below the bf16 output's own 2^-8.  With a scale per slot a probability carries its token's scale into
+// the second product.  FP16 cannot hold such products: a row of zeros has the scale 1 where its neighbours may have
+// 2^-30, and any unit that keeps the one in range loses the others.  They enter in two bf16 parts (2^-17 of each, with
+// FP32's exponents, so that no token's precision depends on another's scale) against V's codes in bf16, one matrix
+// instruction more per fragment.
 //
 // What bounds it: with few rows per head the cache's bytes, with many the matrix instructions and the widening
 // of the codes, which rows_panel does once for 128 rows; with little of either the latency of a range (first
 // pages, first codes, the join).  Measured, heads of 128 (a large copy moves 4.7 TB/s, a large bf16 product makes
-// 1138 TFLOP/s): 64 sequences of 64 heads on 8, a prefix of 65536 and 2048 own tokens, a scale per slot: 237 to 243 us,
-// 590 TFLOP/s in all (the prefix alone 570, with a scale per head 730; the own tokens alone 4.0 to 4.5 TB/s); 64 of
+// 1138 TFLOP/s): 64 sequences of 64 heads on 8, a prefix of 65536 and 2048 own tokens, a scale per slot: 259 us,
+// 545 TFLOP/s in all (the prefix alone 580, with a scale per head 800; the own tokens alone 4.0 to 4.5 TB/s); 64 of
 // 32 heads, 4096 and 512, a scale per head: 28 us, 5 of them the join.
 #include "mixers.h"
 
@@ -29,7 +33,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlock = 32;              // tokens per second product
-constexpr float kOffset = 7.0f;         // log2 of the probabilities' scale
+// log2 of the probabilities' scale.  They exceed it by 2^8 at most: FP16 ends at 2^16, and with a scale per slot none is
+// larger than 1, so that a product with the scale overflows only where the scale does.
+template <bool kTok> constexpr float kOffset = kTok ? -8.0f : 7.0f;
 constexpr float kNegInf = -__builtin_inff();
 
 struct Params {
@@ -57,13 +63,13 @@ template <int D, int NQ> struct Rows {
     float4v o[NQ][D / 16];
     float4v ones[NQ];                   // l as a matrix instruction sums it (a row of ones for V), where it does
     float m[NQ], l[NQ];                 // m: the maximum so far, as far as it was moved
-    float base[NQ];                     // what is added to a score: kOffset - m (kOffset before the first token)
+    float base[NQ];                     // what is added to a score: offset - m (offset before the first token)
     float limit[NQ];                    // above this a score with its base moves the maximum
-    __device__ __forceinline__ void clear() {
+    __device__ __forceinline__ void clear(float offset) {
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             m[n] = limit[n] = kNegInf;
-            base[n] = kOffset;
+            base[n] = offset;
             l[n] = 0.0f;
             ones[n] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -154,12 +160,60 @@ __device__ __forceinline__ float group_sum(float v) {
     return v + __shfl_xor(v, 32, 64);
 }
 
+// V's fragments and the probabilities that meet them: FP16, or with a scale per slot (in the probabilities) bf16, those in
+// two parts.
+template <bool kTok> struct Second;
+template <> struct Second<false> {
+    typedef half8 Values;
+    struct Probs {
+        half8 p;
+        __device__ __forceinline__ void put(int i, float x0, float x1) {
+            p[i] = (_Float16)x0;
+            p[i + 1] = (_Float16)x1;
+        }
+    };
+    static __device__ __forceinline__ Values widen(uint32_t lo, uint32_t hi) { return widen_f16(lo, hi); }
+    static __device__ __forceinline__ uint2 widen4(uint32_t x) {
+        return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, false)),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, true)));
+    }
+    static __device__ __forceinline__ float4v product(Values v, const Probs& p, float4v o) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p.p, o, 0, 0, 0);
+    }
+};
+template <> struct Second<true> {
+    typedef bf16x8 Values;
+    struct Probs {
+        bf16x8 hi, lo;                  // the upper 16 bits as they are, and the nearest bf16 of the rest
+        __device__ __forceinline__ void put(int i, float x0, float x1) {
+            const uint32_t u0 = __float_as_uint(x0), u1 = __float_as_uint(x1);
+            const bf16x2 h = __builtin_bit_cast(bf16x2, __builtin_amdgcn_perm(u1, u0, 0x07060302u));
+            const bf16x2 l = __builtin_convertvector((float2v{x0 - __uint_as_float(u0 & 0xFFFF0000u),
+                                                              x1 - __uint_as_float(u1 & 0xFFFF0000u)}), bf16x2);
+            hi[i] = h[0];
+            hi[i + 1] = h[1];
+            lo[i] = l[0];
+            lo[i + 1] = l[1];
+        }
+    };
+    static __device__ __forceinline__ Values widen(uint32_t lo, uint32_t hi) { return widen_bf16(lo, hi); }
+    static __device__ __forceinline__ uint2 widen4(uint32_t x) {
+        return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, false)),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, true)));
+    }
+    static __device__ __forceinline__ float4v product(Values v, const Probs& p, float4v o) {
+        o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p.lo, o, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p.hi, o, 0, 0, 0);
+    }
+};
+
 // One block's probabilities out of its scores (base 2, with their base added; -inf where nothing counts).  The
-// running maximum is moved only when some score exceeds it by more than 2^8: until then a probability is at most
-// 2^15 in FP16, and no lane has to ask the others for its row's maximum.
-// kScale: the probabilities of the second product carry the values' scales.  kSum: l is summed here.
-template <int D, int NQ, bool kScale, bool kSum>
-__device__ __forceinline__ void softmax_step(Rows<D, NQ>& s, float4v (&sc)[NQ][2], const float4v* vs, half8 (&pf)[NQ]) {
+// running maximum is moved only when some score exceeds it by more than 2^8: until then no lane has to ask the others
+// for its row's maximum.
+// kTok: the probabilities of the second product carry the values' scales vs.  kSum: l is summed here.
+template <int D, int NQ, bool kTok, bool kSum>
+__device__ __forceinline__ void softmax_step(Rows<D, NQ>& s, float4v (&sc)[NQ][2], const float4v* vs,
+                                             typename Second<kTok>::Probs (&pf)[NQ]) {
     bool move = false;
     float mx[NQ];
 #pragma unroll
@@ -173,10 +227,10 @@ __device__ __forceinline__ void softmax_step(Rows<D, NQ>& s, float4v (&sc)[NQ][2
         for (int n = 0; n < NQ; ++n) {
             const float top = group_max(mx[n]) - s.base[n], m_new = fmaxf(s.m[n], top);
             if (m_new > kNegInf) {           // the same for all lanes of a row
-                const float f = __builtin_amdgcn_exp2f(s.m[n] - m_new), base = kOffset - m_new, d = base - s.base[n];
+                const float f = __builtin_amdgcn_exp2f(s.m[n] - m_new), base = kOffset<kTok> - m_new, d = base - s.base[n];
                 s.m[n] = m_new;
                 s.base[n] = base;
-                s.limit[n] = kOffset + 8.0f;
+                s.limit[n] = kOffset<kTok> + 8.0f;
                 if (kSum) s.l[n] *= f;
                 else s.ones[n] *= f;
 #pragma unroll
@@ -194,10 +248,10 @@ __device__ __forceinline__ void softmax_step(Rows<D, NQ>& s, float4v (&sc)[NQ][2
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float e = __builtin_amdgcn_exp2f(sc[n][tt][i]);
-                if (kSum) sum += e;
-                pf[n][4 * tt + i] = (_Float16)(kScale ? e * vs[tt][i] : e);
+            for (int i = 0; i < 4; i += 2) {
+                const float e0 = __builtin_amdgcn_exp2f(sc[n][tt][i]), e1 = __builtin_amdgcn_exp2f(sc[n][tt][i + 1]);
+                if (kSum) sum += e0 + e1;
+                pf[n].put(4 * tt + i, kTok ? e0 * vs[tt][i] : e0, kTok ? e1 * vs[tt][i + 1] : e1);
             }
         if (kSum) s.l[n] += sum;
     }
@@ -218,8 +272,7 @@ __device__ __forceinline__ void walk(const Params& p, int head, const Tokens& li
     const int64_t page_mask = (int64_t(1) << p.page_shift) - 1;
     const int per_head = p.a.cache.scale_mode == NVFP4_KV_SCALE_HEAD ? head : 0;
     const float k_fixed = kTok ? p.scale2 : p.scale2 * p.a.cache.k_scale[per_head];
-    float vmax = 0.0f, vinv = 0.0f;          // per-slot scales: acc counts values in units of vmax
-    s.clear();
+    s.clear(kOffset<kTok>);
     if (t0 < t_end) {
     const int64_t last = (t_end - 1) & ~int64_t(15);
     // A table entry is loaded a block before the codes it leads to and looked at only then: its own latency, and the
@@ -272,23 +325,11 @@ __device__ __forceinline__ void walk(const Params& p, int head, const Tokens& li
                 scales[wave][0][lane] = next_ks * p.scale2;
                 scales[wave][1][lane] = next_vs;
             }
-            if (__builtin_amdgcn_ballot_w64(next_vs > vmax)) {      // a larger unit
-                float vm = fmaxf(vmax, next_vs);
-#pragma unroll
-                for (int off = 1; off < 64; off <<= 1) vm = fmaxf(vm, __shfl_xor(vm, off, 64));
-                vinv = 1.0f / vm;
-                const float f = vmax * vinv;
-#pragma unroll
-                for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) s.o[n][i] *= f;
-                vmax = vm;
-            }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
                 ks[tt] = *reinterpret_cast<const float4v*>(&scales[wave][0][tt * 16 + kg * 4]);
-                vs[tt] = *reinterpret_cast<const float4v*>(&scales[wave][1][tt * 16 + kg * 4]) * vinv;
+                vs[tt] = *reinterpret_cast<const float4v*>(&scales[wave][1][tt * 16 + kg * 4]);
             }
             load_scales(next);
         }
@@ -328,7 +369,7 @@ __device__ __forceinline__ void walk(const Params& p, int head, const Tokens& li
                     for (int j = 0; j < D / 64; ++j) raw.v[tt][i][j] = there ? raw.v[tt][i][j] : 0u;
                 }
         }
-        half8 pf[NQ];
+        typename Second<kTok>::Probs pf[NQ];
         softmax_step<D, NQ, kTok, true>(s, sc, vs, pf);
         // O^T += V^T P^T: tile 4 j + b holds the elements d = row * (D / 16) + 4 j + b
 #pragma unroll
@@ -338,10 +379,9 @@ __device__ __forceinline__ void walk(const Params& p, int head, const Tokens& li
             transpose4(raw.v[1][0][j], raw.v[1][1][j], raw.v[1][2][j], raw.v[1][3][j], hi);
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                const half8 vf = widen_f16(lo[b], hi[b]);
+                const auto vf = Second<kTok>::widen(lo[b], hi[b]);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n)
-                    s.o[n][4 * j + b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[n], s.o[n][4 * j + b], 0, 0, 0);
+                for (int n = 0; n < NQ; ++n) s.o[n][4 * j + b] = Second<kTok>::product(vf, pf[n], s.o[n][4 * j + b]);
             }
         }
 #pragma unroll
@@ -351,7 +391,7 @@ __device__ __forceinline__ void walk(const Params& p, int head, const Tokens& li
         }
     }
     }
-    const float unit = kTok ? vmax : p.a.cache.v_scale[per_head];
+    const float unit = kTok ? 1.0f : p.a.cache.v_scale[per_head];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
         s.l[n] = group_sum(s.l[n]);
@@ -447,16 +487,15 @@ __device__ __forceinline__ void rows_shared(const Params& p, int head, int base_
 
 // Many rows over a long prefix (head_dim 64 and 128): a workgroup whose wavefronts take 16 NQ rows each, all over the
 // same tokens.  The codes of 64 tokens are widened once for the four wavefronts, into LDS in the order of the
-// fragments: K [token][d] in bf16, V [d][token] in FP16 with each 32 tokens in the order of the scores' registers and
+// fragments: K [token][d] in bf16, V [d][token] (FP16, or bf16 with a scale per slot) with each 32 tokens in the order of the scores' registers and
 // the 16-byte units of a row exchanged by its number, so that neither the writes (eight rows apart) nor the reads
 // (neighbouring rows) meet on a bank.  Two blocks in LDS, one barrier per block.
 constexpr int kPanel = 64;
 
 template <int D> struct Panels {
     alignas(16) __bf16 k[2][kPanel][D + 8];
-    alignas(16) _Float16 v[2][D][kPanel];
-    alignas(16) float scales[2][kPanel];     // K's per-slot scales
-    float top[4];
+    alignas(16) uint16_t v[2][D][kPanel];
+    alignas(16) float scales[2][2][kPanel];  // the per-slot scales of K and V
 };
 
 __device__ __forceinline__ int panel_unit(int d, int unit) { return (unit ^ d ^ (d >> 3)) & 7; }
@@ -475,34 +514,16 @@ __device__ __forceinline__ void rows_panel(const Params& p, int head, int row0, 
     for (int n = 0; n < NQ; ++n)             // in the natural order of d here
         load_queries<D, true>(p, head, 0, row0 + 16 * n, rows_total, qf[n]);
     Rows<D, NQ> s;
-    s.clear();
+    s.clear(kOffset<kTok>);
     const int64_t page_mask = (int64_t(1) << p.page_shift) - 1;
     const int per_head = p.a.cache.scale_mode == NVFP4_KV_SCALE_HEAD ? head : 0;
     const float k_fixed = kTok ? 1.0f : p.scale2 * p.a.cache.k_scale[per_head];
-    // Per-slot scales of V go into its panel, in units of the range's largest: there they cost a product per value
-    // and workgroup, in the probabilities one per token, row and wavefront.  V is then rounded to FP16 (2^-11), with a
-    // factor of 2^7 that keeps rows of small scales (to 2^-21 of the largest) in the format's normal range.
-    float unit = kTok ? 0.0f : p.a.cache.v_scale[per_head], vfactor = 0.0f;
-    if constexpr (kTok) {
-        float top = 0.0f;
-        for (int64_t t = t0 + (int)threadIdx.x; t < t_end; t += kThreads) {
-            const int32_t page = pages[t >> p.page_shift];
-            if (page >= 0 && page < p.a.cache.pages)
-                top = fmaxf(top, p.a.cache.v_scale[(((int64_t)page << p.page_shift) + (t & page_mask)) * p.a.cache.heads + head]);
-        }
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-        if (lane == 0) sh.top[wave] = top;
-        __syncthreads();
-        top = fmaxf(fmaxf(sh.top[0], sh.top[1]), fmaxf(sh.top[2], sh.top[3]));
-        unit = top * 0.0078125f;
-        vfactor = top > 0.0f ? 128.0f / top : 0.0f;
-    }
+    const float unit = kTok ? 1.0f : p.a.cache.v_scale[per_head];
     const int64_t last = (t_end - 1) & ~int64_t(15);
     // this wavefront's 16 tokens of a block
     uint4 rk[D / 64];
     uint32_t rv[4][D / 64];
-    float rks = 0.0f, rvs[4] = {};
+    float rks = 0.0f, rvs = 0.0f;
     int live = 0;
     auto entry = [&](int64_t b) { return pages[(b < last ? b : last) >> p.page_shift]; };
     auto find = [&](int64_t b, int32_t e, int& n) {      // as in walk
@@ -517,10 +538,9 @@ __device__ __forceinline__ void rows_panel(const Params& p, int head, int row0, 
         load_k<D>(p, head, slot0, l16, kg, rk);
         load_v<D>(p, head, slot0, l16, kg, rv);
         if constexpr (kTok) {
-            const int64_t at = slot0 * p.a.cache.heads + head;
-            rks = p.a.cache.k_scale[at + (uint32_t)(l16 * p.a.cache.heads)];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rvs[i] = p.a.cache.v_scale[at + (uint32_t)((4 * kg + i) * p.a.cache.heads)];
+            const int64_t at = (slot0 + l16) * p.a.cache.heads + head;
+            rks = p.a.cache.k_scale[at];
+            rvs = p.a.cache.v_scale[at];
         }
     };
     load(find(t0 + 16 * wave, entry(t0 + 16 * wave), live));
@@ -539,11 +559,7 @@ __device__ __forceinline__ void rows_panel(const Params& p, int head, int row0, 
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < D / 64; ++j) rv[i][j] = 4 * kg + i < live ? rv[i][j] : 0u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rvs[i] = 4 * kg + i < live ? rvs[i] : 0.0f;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rvs[i] *= vfactor;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
             uint32_t y[4];
@@ -551,22 +567,15 @@ __device__ __forceinline__ void rows_panel(const Params& p, int head, int row0, 
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const int d = l16 * (D / 16) + 4 * j + b;
-                half2v lo, hi;
-                if constexpr (kTok) {
-                    const float2v a = __builtin_amdgcn_cvt_pk_f32_fp8((int)y[b], false), c = __builtin_amdgcn_cvt_pk_f32_fp8((int)y[b], true);
-                    lo = __builtin_convertvector((float2v{a[0] * rvs[0], a[1] * rvs[1]}), half2v);
-                    hi = __builtin_convertvector((float2v{c[0] * rvs[2], c[1] * rvs[3]}), half2v);
-                } else {
-                    lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y[b], 1.0f, false);
-                    hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y[b], 1.0f, true);
-                }
-                typedef _Float16 half4 __attribute__((ext_vector_type(4)));
-                *reinterpret_cast<half4*>(&sh.v[buf][d][panel_unit(d, (wave >> 1) * 4 + kg) * 8 + (wave & 1) * 4]) =
-                    half4{lo[0], lo[1], hi[0], hi[1]};
+                *reinterpret_cast<uint2*>(&sh.v[buf][d][panel_unit(d, (wave >> 1) * 4 + kg) * 8 + (wave & 1) * 4]) =
+                    Second<kTok>::widen4(y[b]);
             }
         }
         if constexpr (kTok) {
-            if (kg == 0) sh.scales[buf][wave * 16 + l16] = l16 < live ? rks * p.scale2 : 0.0f;
+            if (kg == 0) {
+                sh.scales[buf][0][wave * 16 + l16] = l16 < live ? rks * p.scale2 : 0.0f;
+                sh.scales[buf][1][wave * 16 + l16] = l16 < live ? rvs : 0.0f;
+            }
         }
         // tokens that do not count: at the end of the range, or a page outside the pool (whose half block says so)
         if (lane == 0) reinterpret_cast<int*>(&sh.k[buf][wave * 16][D])[0] = live;
@@ -591,11 +600,15 @@ __device__ __forceinline__ void rows_panel(const Params& p, int head, int row0, 
         }
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
+            float4v vs[2];
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
                 const int tile = st * 2 + tt;
                 float4v ks;
-                if constexpr (kTok) ks = *reinterpret_cast<const float4v*>(&sh.scales[buf][tile * 16 + kg * 4]);
+                if constexpr (kTok) {
+                    ks = *reinterpret_cast<const float4v*>(&sh.scales[buf][0][tile * 16 + kg * 4]);
+                    vs[tt] = *reinterpret_cast<const float4v*>(&sh.scales[buf][1][tile * 16 + kg * 4]);
+                }
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -608,24 +621,26 @@ __device__ __forceinline__ void rows_panel(const Params& p, int head, int row0, 
                         for (int i = 0; i < 4; ++i) sc[st][n][tt][i] = 4 * kg + i < count ? sc[st][n][tt][i] : kNegInf;
                 }
             }
-            half8 pf[NQ];
-            softmax_step<D, NQ, false, false>(s, sc[st], nullptr, pf);
-            const _Float16 one = (_Float16)1.0f;
-            const half8 ones = {one, one, one, one, one, one, one, one};
+            typename Second<kTok>::Probs pf[NQ];
+            softmax_step<D, NQ, kTok, kTok>(s, sc[st], vs, pf);
+            if constexpr (!kTok) {
+                const _Float16 one = (_Float16)1.0f;
+                const half8 ones = {one, one, one, one, one, one, one, one};
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) s.ones[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pf[n], s.ones[n], 0, 0, 0);
+                for (int n = 0; n < NQ; ++n) s.ones[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pf[n].p, s.ones[n], 0, 0, 0);
+            }
 #pragma unroll
             for (int m = 0; m < D / 16; ++m) {
                 const int d = m * 16 + l16;
-                const half8 vf = *reinterpret_cast<const half8*>(&sh.v[buf][d][panel_unit(d, st * 4 + kg) * 8]);
+                const auto vf = *reinterpret_cast<const typename Second<kTok>::Values*>(&sh.v[buf][d][panel_unit(d, st * 4 + kg) * 8]);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) s.o[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[n], s.o[n][m], 0, 0, 0);
+                for (int n = 0; n < NQ; ++n) s.o[n][m] = Second<kTok>::product(vf, pf[n], s.o[n][m]);
             }
         }
     }
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-        s.l[n] = s.ones[n][0];
+        s.l[n] = kTok ? group_sum(s.l[n]) : s.ones[n][0];
         const int row = row0 + 16 * n + l16;
         if (!any || row >= rows_total) continue;
         const int b = row / p.a.group, hq = head * p.a.group + row % p.a.group;
