@@ -623,8 +623,14 @@ nvfp4_status nvfp4_prefix_attention(const nvfp4_kv_cache* cache, const void* q, 
  *          k_heads, <= 65535; batch * v_heads <= 2^18, times tokens <= 2^34
  * k_dim  : a multiple of 32, 32 .. 128;  v_dim: a multiple of 16, 16 .. 256
  * q, k   : bf16 rows of k_dim on 16-byte boundaries;  v: bf16 rows of v_dim
- * alpha, beta : FP32, one value per (batch, token, value head); any finite
- *          values (0 included), meant for [0, 1]
+ * alpha, beta : FP32, one value per (batch, token, value head), with
+ *          -1 <= alpha <= 1 and 0 <= beta |k|^2 <= 2 (both ends included): then
+ *          no update lengthens the state, and the precision above holds.
+ *          Gates outside are not refused.  Up to 8 tokens they are simply
+ *          multiplied in; a longer forward call, and every backward call, forms
+ *          products of up to 64 of them apart from the state, loses what
+ *          these exceed the states by, and gives infinities or NaN where they
+ *          leave FP32's range, also where the recurrence itself would not
  * lens   : device, int32 [batch], or NULL: row b has its first lens[b] tokens
  *          (clamped to 0 .. tokens); what the others hold is not used, and their
  *          rows of every output are left as they were

@@ -621,7 +621,9 @@ def _gdn_state(x, name, shape, device):
 def gdn_desc(q, k, v, alpha, beta, scale=None, state=None, lens=None) -> GdnDesc:
     """The descriptor of a gated delta recurrence: q, k [batch, tokens, k_heads, k_dim] and v [batch, tokens, v_heads,
     v_dim] bfloat16, alpha and beta [batch, tokens, v_heads] float32 (the gates), state [batch, v_heads, k_dim, v_dim]
-    float32 or None (zeros), lens int32 [batch] or None; scale defaults to k_dim ** -0.5.  It holds their addresses."""
+    float32 or None (zeros), lens int32 [batch] or None; scale defaults to k_dim ** -0.5.  The gates are meant for
+    -1 <= alpha <= 1 and 0 <= beta |k|^2 <= 2 (no update lengthens the state); more than 8 tokens, and gradients, lose
+    precision outside, and overflow where a product of 64 of them does.  It holds their addresses."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q and v must be [batch, tokens, heads, dim]")
     b, t, hk, dk = q.shape

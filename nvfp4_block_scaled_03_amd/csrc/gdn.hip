@@ -22,6 +22,8 @@
 // operands, so every FP32 operand is split into three bf16 parts (24 significant bits, what FP32 holds): a
 // product with q, k, v or dO, exact in bf16, takes three instructions, one of two FP32 operands the six
 // whose parts reach 2^-24; gfx950's FP32 matrix instruction would take the time of sixteen.
+// The products of decays and T stand apart from the state, so this holds where they are no larger than 1 or so: for
+// |alpha| <= 1 and 0 <= beta |k|^2 <= 2, where no factor alpha (I - beta k k^T) lengthens what it acts on.
 #include "mixers.h"
 
 namespace nvfp4 {
