@@ -283,23 +283,22 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torc
 
 class _Launch:
     """Around a launch on a tensor's device: that device is made current if it is not, and ``stream`` (None: its current
-    stream) is what ``with`` gives, as a pointer."""
+    stream) is what ``with`` gives, as a pointer.  Addresses of host memory, which would fault the GPU, are refused."""
     __slots__ = ("device", "stream", "previous")
 
     def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on a GPU, not on {device}")
         self.device, self.stream, self.previous = device, stream, None
 
     def __enter__(self):
-        if self.device.type == "cuda":
-            current = torch.cuda.current_device()
-            index = self.device.index
-            if index is not None and index != current:
-                self.previous = current
-                torch.cuda.set_device(index)
-                current = index
-            if self.stream is None:
-                return _raw_stream(current)
-        return _stream(self.stream)
+        current = torch.cuda.current_device()
+        index = self.device.index
+        if index is not None and index != current:
+            self.previous = current
+            torch.cuda.set_device(index)
+            current = index
+        return _raw_stream(current) if self.stream is None else _stream(self.stream)
 
     def __exit__(self, *exc):
         if self.previous is not None:

@@ -1,0 +1,34 @@
+"""Where the tensors of the cache, attention and the recurrence are: calls that would give a kernel addresses that are
+not the GPU's are refused before anything is launched."""
+import pytest
+import torch
+
+import nvfp4_block_scaled_03_amd as nv
+
+BF16 = torch.bfloat16
+
+
+def _cache():
+    return nv.KVCache.allocate(4, 16, 2, 64, device="cpu")
+
+
+def _gdn(t):
+    q, v = torch.zeros(2, t, 1, 32).to(BF16), torch.zeros(2, t, 2, 16).to(BF16)
+    return q, q, v, torch.zeros(2, t, 2), torch.zeros(2, t, 2)
+
+
+HOST_CALLS = {
+    "write": lambda: nv.kv_cache_write(torch.zeros(3, 2, 64), torch.zeros(3, 2, 64), _cache(), torch.arange(3)),
+    "read": lambda: nv.kv_cache_read(_cache(), torch.arange(3)),
+    "attention": lambda: nv.prefix_attention(torch.zeros(2, 4, 64).to(BF16), _cache(), torch.zeros(1, dtype=torch.int32), 5,
+                                             torch.ones(2, 1, dtype=torch.int32), torch.ones(2, dtype=torch.int32)),
+    "step": lambda: nv.gdn_forward(*_gdn(1)),
+    "forward": lambda: nv.gdn_forward(*_gdn(70)),
+    "backward": lambda: nv.gdn_backward(*_gdn(70), _gdn(70)[2]),
+}
+
+
+@pytest.mark.parametrize("name", sorted(HOST_CALLS))
+def test_host_tensors_are_refused(name):
+    with pytest.raises(ValueError, match="GPU"):
+        HOST_CALLS[name]()
