@@ -520,6 +520,17 @@ def _check_ints(t, what, dtype, dims, device):
         raise ValueError(f"{what} is on {t.device}, the cache on {device}")
 
 
+def _workspace_size(workspace, device):
+    """Bytes of a workspace tensor (0 for none), which has to be contiguous and where the call runs."""
+    if not isinstance(workspace, torch.Tensor):
+        return 0
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, the call on {device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def nvfp4_kv_cache_write(cache: "KVCache", k, v, slots, stream=None):
     """Quantize rows k, v [tokens, heads, head_dim] (float32 or bfloat16) into the cache at slots (int64)."""
     _check_ints(slots, "slots", torch.int64, 1, cache.device)
@@ -580,7 +591,7 @@ def nvfp4_prefix_attention(cache: "KVCache", q, prefix_pages, prefix_len: int, p
         max_len = n_pages * cache.page_size
     qp, qb, qh = _rows3(q, "q")
     op, ob, oh = _rows3(out, "out")
-    ws_bytes = workspace.numel() * workspace.element_size() if isinstance(workspace, torch.Tensor) else 0
+    ws_bytes = _workspace_size(workspace, cache.device)
     with _Launch(cache.device, stream) as on:
         _check(_lib.nvfp4_prefix_attention(cache.ref, qp, qb, qh, batch, heads, dim ** -0.5 if scale is None else scale,
                                            _ptr(prefix_pages) if prefix_len > 0 else None, prefix_len, _ptr(pages),
@@ -654,7 +665,7 @@ def nvfp4_gdn_forward(g: GdnDesc, o, state_out=None, workspace=None, stream=None
     dev = getattr(g, "device", o.device)
     rows = RowsDesc(*_gdn_rows(o, "o", (g.batch, g.tokens, g.v_heads, g.v_dim), torch.bfloat16, dev))
     so = _gdn_state(state_out, "state_out", (g.batch, g.v_heads, g.k_dim, g.v_dim), dev)
-    ws_bytes = workspace.numel() * workspace.element_size() if isinstance(workspace, torch.Tensor) else 0
+    ws_bytes = _workspace_size(workspace, dev)
     with _Launch(dev, stream) as on:
         _check(_lib.nvfp4_gdn_forward(ctypes.byref(g), ctypes.byref(rows), so, _ptr(workspace), ws_bytes,
                                       on))
@@ -672,7 +683,7 @@ def nvfp4_gdn_backward(g: GdnDesc, d_o, d_state_out, d_q, d_k, d_v, d_log_alpha,
         (d_beta, "d_beta", (b, t, hv), f32))]
     dso = _gdn_state(d_state_out, "d_state_out", (b, hv, dk, dv), dev)
     ds = _gdn_state(d_state, "d_state", (b, hv, dk, dv), dev)
-    ws_bytes = workspace.numel() * workspace.element_size() if isinstance(workspace, torch.Tensor) else 0
+    ws_bytes = _workspace_size(workspace, dev)
     with _Launch(dev, stream) as on:
         _check(_lib.nvfp4_gdn_backward(ctypes.byref(g), ctypes.byref(rows[0]), dso, *[ctypes.byref(r) for r in rows[1:]],
                                        ds, _ptr(workspace), ws_bytes, on))

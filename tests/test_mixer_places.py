@@ -32,3 +32,17 @@ HOST_CALLS = {
 def test_host_tensors_are_refused(name):
     with pytest.raises(ValueError, match="GPU"):
         HOST_CALLS[name]()
+
+
+@pytest.mark.parametrize("workspace", [torch.empty(1 << 22, dtype=torch.uint8, device="meta"),
+                                       torch.empty(1, dtype=torch.uint8).expand(1 << 22)], ids=["elsewhere", "one_byte"])
+def test_workspaces_elsewhere_or_not_whole_are_refused(workspace):
+    cache, t = _cache(), _gdn(70)
+    table, lens = torch.ones(2, 1, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="workspace"):
+        nv.prefix_attention(torch.zeros(2, 4, 64).to(BF16), cache, torch.zeros(1, dtype=torch.int32), 5, table, lens,
+                            workspace=workspace)
+    with pytest.raises(ValueError, match="workspace"):
+        nv.gdn_forward(*t, workspace=workspace)
+    with pytest.raises(ValueError, match="workspace"):
+        nv.gdn_backward(*t, t[2], workspace=workspace)
