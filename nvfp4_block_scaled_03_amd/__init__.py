@@ -498,12 +498,13 @@ def nvfp4_linear_noalloc(x, x_codes, x_scales, g_x, desc: WeightDesc, y, g_mode=
 
 
 def _rows3(x, name):
-    """(data pointer, token stride, head stride) of a [tokens, heads, dim] tensor with unit last stride."""
+    """(data pointer, token stride, head stride) of a [tokens, heads, dim] tensor with unit last stride.  The stride of
+    an axis of one entry is arbitrary: the row's size stands for it."""
     tokens, heads, dim = x.shape
     st, sh, sd = x.stride()
     if dim > 1 and sd != 1:
         raise ValueError(f"{name} must have unit stride along its last axis")
-    return x.data_ptr(), (st if tokens > 1 else max(st, dim)), (sh if heads > 1 else max(sh, dim))
+    return x.data_ptr(), (st if tokens > 1 else dim), (sh if heads > 1 else dim)
 
 
 def _rows_match(cache, what, x, slots):
@@ -613,7 +614,7 @@ def _gdn_rows(x, name, shape, dtype, device):
         dim = shape[3]
         if dim > 1 and stride[3] != 1:
             raise ValueError(f"{name} must have unit stride along its last axis")
-    return x.data_ptr(), stride[0], stride[1], stride[2] if shape[2] > 1 else max(stride[2], dim)
+    return x.data_ptr(), stride[0], stride[1], stride[2] if shape[2] > 1 else dim    # one head's is arbitrary
 
 
 def _gdn_state(x, name, shape, device):

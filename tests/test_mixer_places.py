@@ -46,3 +46,15 @@ def test_workspaces_elsewhere_or_not_whole_are_refused(workspace):
         nv.gdn_forward(*t, workspace=workspace)
     with pytest.raises(ValueError, match="workspace"):
         nv.gdn_backward(*t, t[2], workspace=workspace)
+
+
+def test_strides_of_single_entries_do_not_count():
+    """An axis of one entry may have any stride; what the kernels are told for it is the row's size."""
+    one = torch.as_strided(torch.zeros(64).to(BF16), (1, 1, 64), (4099, 3, 1))
+    assert nv._rows3(one, "q")[1:] == (64, 64)
+    rows = torch.as_strided(torch.zeros(4096).to(BF16), (3, 1, 64), (128, 68, 1))
+    assert nv._rows3(rows, "q")[1:] == (128, 64)
+    x = torch.as_strided(torch.zeros(4096).to(BF16), (1, 3, 1, 64), (9, 128, 68, 1))
+    assert nv._gdn_rows(x, "q", (1, 3, 1, 64), BF16, x.device)[2:] == (128, 64)
+    gates = torch.as_strided(torch.zeros(64), (1, 3, 1), (0, 5, 0))
+    assert nv._gdn_rows(gates, "alpha", (1, 3, 1), torch.float32, gates.device)[2:] == (5, 1)
