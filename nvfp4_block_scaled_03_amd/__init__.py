@@ -634,7 +634,7 @@ def gdn_desc(q, k, v, alpha, beta, scale=None, state=None, lens=None) -> GdnDesc
     v_dim] bfloat16, alpha and beta [batch, tokens, v_heads] float32 (the gates), state [batch, v_heads, k_dim, v_dim]
     float32 or None (zeros), lens int32 [batch] or None; scale defaults to k_dim ** -0.5.  The gates are meant for
     -1 <= alpha <= 1 and 0 <= beta |k|^2 <= 2 (no update lengthens the state); more than 8 tokens, and gradients, lose
-    precision outside, and overflow where a product of 64 of them does.  It holds their addresses."""
+    precision outside, and overflow where a product of 64 of them does.  It holds the tensors it points to."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q and v must be [batch, tokens, heads, dim]")
     b, t, hk, dk = q.shape
@@ -649,7 +649,7 @@ def gdn_desc(q, k, v, alpha, beta, scale=None, state=None, lens=None) -> GdnDesc
                 _gdn_rows(v, "v", (b, t, hv, dv), bf16, dev), _gdn_rows(alpha, "alpha", (b, t, hv), f32, dev),
                 _gdn_rows(beta, "beta", (b, t, hv), f32, dev), _ptr(lens),
                 _gdn_state(state, "state", (b, hv, dk, dv), dev))
-    g.device = dev
+    g.device, g.tensors = dev, (q, k, v, alpha, beta, state, lens)
     return g
 
 

@@ -1,5 +1,7 @@
 """Where the tensors of the cache, attention and the recurrence are: calls that would give a kernel addresses that are
 not the GPU's are refused before anything is launched."""
+import weakref
+
 import pytest
 import torch
 
@@ -58,3 +60,15 @@ def test_strides_of_single_entries_do_not_count():
     assert nv._gdn_rows(x, "q", (1, 3, 1, 64), BF16, x.device)[2:] == (128, 64)
     gates = torch.as_strided(torch.zeros(64), (1, 3, 1), (0, 5, 0))
     assert nv._gdn_rows(gates, "alpha", (1, 3, 1), torch.float32, gates.device)[2:] == (5, 1)
+
+
+def test_a_descriptor_holds_what_it_points_to():
+    """Made from temporaries, it must not be left with addresses that the allocator hands out again."""
+    q, k, v, alpha, beta = _gdn(5)
+    state, lens = torch.zeros(2, 2, 32, 16), torch.zeros(2, dtype=torch.int32)
+    alive = [weakref.ref(x) for x in (q, v, alpha, beta, state, lens)]
+    g = nv.gdn_desc(q, k, v, alpha, beta, state=state, lens=lens)
+    del q, k, v, alpha, beta, state, lens
+    assert all(r() is not None for r in alive)
+    del g
+    assert all(r() is None for r in alive)
