@@ -515,7 +515,7 @@ def _rows_match(cache, what, x, slots):
 
 
 def _check_ints(t, what, dtype, dims, device):
-    if t.dtype != dtype or t.dim() != dims or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dims or not t.is_contiguous():
         raise TypeError(f"{what} must be a contiguous {dims}-D {dtype} tensor")
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, the cache on {device}")

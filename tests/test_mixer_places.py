@@ -72,3 +72,13 @@ def test_a_descriptor_holds_what_it_points_to():
     assert all(r() is not None for r in alive)
     del g
     assert all(r() is None for r in alive)
+
+
+def test_missing_tables_are_named():
+    cache, q = _cache(), torch.zeros(2, 4, 64).to(BF16)
+    table, lens = torch.ones(2, 1, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    for pre, pages, n, name in ((None, table, lens, "prefix_pages"), (table[0], table, None, "lens")):
+        with pytest.raises(TypeError, match=name):
+            nv.prefix_attention(q, cache, pre, 5, pages, n)
+    with pytest.raises(TypeError, match="slots"):
+        nv.kv_cache_write(q[:, :2], q[:, :2], cache, [0, 1])
