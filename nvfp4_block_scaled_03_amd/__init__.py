@@ -249,15 +249,15 @@ def _stream(stream):
 
 
 def _on_stream(stream):
-    """Context for the conveniences below when the caller names a stream: the stream first waits for the
-    current stream (whose work produced the inputs), and every allocation and fill inside runs on it, so
+    """Context for the conveniences below when the caller names a stream: the stream first waits for its
+    device's current stream (whose work produced the inputs), and every allocation and fill inside runs on it, so
     temporaries (workspaces, g) are ordered with the launches that use them and are only reused by the
     caching allocator after that stream's work.  No stream: the current one, nothing to do."""
     import contextlib
     if stream is None:
         return contextlib.nullcontext()
     s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-    s.wait_stream(torch.cuda.current_stream())
+    s.wait_stream(torch.cuda.current_stream(s.device))
     return torch.cuda.stream(s)
 
 

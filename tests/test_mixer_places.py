@@ -82,3 +82,17 @@ def test_missing_tables_are_named():
             nv.prefix_attention(q, cache, pre, 5, pages, n)
     with pytest.raises(TypeError, match="slots"):
         nv.kv_cache_write(q[:, :2], q[:, :2], cache, [0, 1])
+
+
+def test_a_stream_waits_for_its_own_device(monkeypatch):
+    """A stream of another device than the current one waits for what produced the inputs there."""
+    class Stream:
+        device, waited = torch.device("cuda:1"), []
+
+        def wait_stream(self, other):
+            self.waited.append(other)
+
+    s = Stream()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: ("current", device))
+    monkeypatch.setattr(torch.cuda, "stream", lambda x: ("on", x))
+    assert nv._on_stream(s) == ("on", s) and s.waited == [("current", torch.device("cuda:1"))]
