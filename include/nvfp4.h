@@ -601,10 +601,15 @@ nvfp4_status nvfp4_prefix_attention(const nvfp4_kv_cache* cache, const void* q, 
                                     size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
- * The gated delta recurrence of a Gated DeltaNet layer, the consumer of the
- * fused projection's q, k, v and of the gates that nvfp4_linear_gated and
- * nvfp4_gemm_gated write (decay alpha, write strength beta; anthology-of-the-
+ * The gated delta recurrence of a Gated DeltaNet layer, over the q, k and v that
+ * the layer makes of its fused projection and the gates that nvfp4_linear_gated
+ * and nvfp4_gemm_gated write (decay alpha, write strength beta; anthology-of-the-
  * sota record theory-128, Kozyrev and Maiboroda 2026, section "The account").
+ * Those calls write all of Y in one type, and the recurrence takes two: the
+ * gates' columns of an FP32 Y are read where they are, q, k and v are bf16, as
+ * the layer's normalisation of q and k or its convolution leaves them (or a
+ * cast); the gates of a bf16 Y have lost the decay (0.9995 rounds to 1) and are
+ * not taken.
  * Per batch row and value head, with a state S [k_dim][v_dim] in FP32:
  *
  *   S_t = alpha_t (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T
@@ -617,7 +622,7 @@ nvfp4_status nvfp4_prefix_attention(const nvfp4_kv_cache* cache, const void* q, 
  * parts (24 bits), so states and gate gradients keep FP32's precision.
  *
  * A view nvfp4_rows is [batch][tokens][heads] rows of unit stride with strides
- * in elements, so column slices of the projection's output need no copy.  No
+ * in elements, so column slices of a wider row of that type need no copy.  No
  * stride is less than the row; a token's is at most 2^23.
  * batch  : 0 .. 65535;  tokens: 0 .. 2^28;  k_heads >= 1; v_heads a multiple of
  *          k_heads, <= 65535; batch * v_heads <= 2^18, times tokens <= 2^34
