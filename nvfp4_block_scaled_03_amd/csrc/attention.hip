@@ -766,12 +766,18 @@ Plan plan(int heads, int dim, int64_t batch, int64_t group, int64_t prefix_len, 
     Plan q{};
     const int64_t rows = batch * group;
     // Panels widen a code once for 128 rows instead of once for 16, but fill the chip with an eighth of the workgroups
-    // and cost a start of their own.  8 heads of 128 (narrow, wide, us): a prefix of 16384 64 rows 21.8, 25.0; 96 rows
-    // 27.7, 26.6; 256 rows 53.4, 37.0; of 4096 128 rows 16.5, 20.2; 256 rows 22.7, 23.8, with 512 own tokens 31.3, 27.7,
-    // with a scale per slot 27.1, 25.8; 384 rows 33.7, 29.3; of 65536 48 rows 45.7, 55.0; 64 rows 54.7, 52.1.  So the
-    // products (rows * heads * prefix_len) decide, from three quarters of a panel on.  head_dim 256 has no panels (K and
-    // V of two blocks are more than the LDS holds).
-    q.wide = dim != 256 && rows >= kWideRows * 3 / 4 && rows * heads * prefix_len >= int64_t(8) << 20;
+    // and cost a start of their own, which workgroups over own tokens can fill.  So the products (rows * heads *
+    // prefix_len) decide, from three quarters of a panel on, earlier with own tokens.  Time of panels over that of tiles,
+    // 96 to 512 rows of 2 and 8 heads of 128 and 8 of 64, a scale per head (per slot):
+    //   without own tokens  8 << 20: +1 to +24% (-2 to +22);  12 << 20: -9 to +17 (-16 to +16);  16 << 20: -14 to +6
+    //                       (-22 to +2);  32 << 20: -31 to -14 (-35 to -18)
+    //   with 128            8 << 20: -10 to +22 (-16 to +15)
+    //   with 512            6 << 20: -16 to +6 (-15 to +5);  8 << 20: -14 to +11 (-18 to +2)
+    //   with 2048           6 << 20: -10 to +12 (-9 to +2);  8 << 20: -20 to +8 (-12 to +4)
+    // 64 rows: -3 to +31% (-6 to +28) at 8 and 16 << 20.  head_dim 256 has no panels (K and V of two blocks are more than the
+    // LDS holds).
+    q.wide = dim != 256 && rows >= kWideRows * 3 / 4 &&
+             rows * heads * prefix_len >= (max_len >= 256 ? int64_t(7) << 20 : int64_t(12) << 20);
     q.prefix_tiles = (int)ceil_div(rows, q.wide ? kWideRows : 16);
     q.prefix_range = q.seq_range = kBlock;
     // A prefix so short that each sequence walks it itself, eight blocks of 32 per wavefront at most: one launch and

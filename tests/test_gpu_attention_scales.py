@@ -19,8 +19,8 @@ LAYOUTS = {
     "ranges": (4, 1, 4, 128, 3000, 1500, 64),          # prefix and own tokens in several ranges, joined
     "ranges_256": (5, 1, 4, 256, 2100, 40, 64),
     "own_only": (2, 2, 2, 128, 0, 1300, 16),
-    "panels": (1, 1, 128, 128, 70001, 37, 64),         # codes of the prefix widened once for 128 rows
-    "panels_64": (2, 1, 64, 64, 67000, 20, 16),
+    "panels": (1, 1, 128, 128, 57411, 300, 64),        # codes of the prefix widened once for 128 rows
+    "panels_64": (2, 1, 64, 64, 57411, 290, 16),
 }
 
 

@@ -96,3 +96,25 @@ def test_a_stream_waits_for_its_own_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: ("current", device))
     monkeypatch.setattr(torch.cuda, "stream", lambda x: ("on", x))
     assert nv._on_stream(s) == ("on", s) and s.waited == [("current", torch.device("cuda:1"))]
+
+
+def test_panels_pay_earlier_beside_own_tokens():
+    """The split of a prefix, as its workspace shows it: many rows take panels (ranges of 256 tokens, one workgroup for
+    128 rows) from 12 << 20 products of rows, heads and tokens on, from 7 << 20 with 256 own tokens or more."""
+    def ranges(rows, prefix, max_len, dim=128):
+        cache = nv.KVCache.allocate(1, 16, 8, dim, device="cpu")
+        size = nv.nvfp4_prefix_attention_workspace_bytes(cache, rows // 4, 32, prefix, max_len)
+        own = 0 if max_len == 0 else max(1, min(1024 // (8 * rows // 4), -(-max_len // 512)))
+        for n in range(1, 600):
+            ml = -(-rows * 8 * n * 8 // 256) * 256
+            if n > 1 and size == ml + rows * 8 * n * dim * 4:
+                return n - own
+        return 1
+
+    tiles = {rows: max(1, 512 // (8 * -(-rows // 16))) for rows in (64, 80, 96, 256)}
+    for rows, max_len, least in ((96, 0, 12), (256, 0, 12), (96, 255, 12), (96, 256, 7), (256, 512, 7)):
+        edge = -(-(least << 20) // (rows * 8))
+        assert ranges(rows, edge, max_len) > ranges(rows, edge - 1, max_len) == tiles[rows], (rows, max_len)
+    for rows in (64, 80):                                   # less than three quarters of a panel
+        assert ranges(rows, 65536, 0) == tiles[rows]
+    assert ranges(256, 65536, 0, dim=256) == tiles[256]
