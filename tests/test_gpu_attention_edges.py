@@ -11,7 +11,7 @@ OWN = [260, 0, 1, 17, 255]
 
 @pytest.mark.parametrize("mode", MODES)
 @pytest.mark.parametrize("batch,group,prefix,lens", [
-    (6, 16, 76459, OWN + [64]), (6, 16, 76460, OWN + [64]),      # one product short of 7 << 20, and there
+    (6, 16, 76458, OWN + [64]), (6, 16, 76459, OWN + [64]),      # one token short of 7 << 20, and there
     (5, 19, 77300, OWN),                                         # 95 rows
     (4, 32, 57344, [0, 1, 17, 240]), (4, 32, 57344, [0, 1, 17, 241]),   # a table of 240, of 256 own tokens
     (2, 64, 98304, [5, 0]), (2, 64, 98303, [5, 0])])             # 12 << 20
