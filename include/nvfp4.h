@@ -584,7 +584,8 @@ nvfp4_status nvfp4_kv_cache_read(const nvfp4_kv_cache* cache, int64_t tokens, co
  * lens         : device, int32 [batch]; values above max_len count as max_len,
  *                negative ones as 0
  * max_len      : 0 .. pages_ld * page_size: the host's bound on lens (sizes the
- *                launch; a captured graph holds for all lens up to it)
+ *                launch; a captured graph holds for all lens up to it; a
+ *                bound far above the lengths leaves part of the launch idle)
  * A page number outside the pool drops its tokens from the sums.  What the last
  * page holds behind a sequence's last token is never used, whatever it is.
  * workspace    : device, >= nvfp4_prefix_attention_workspace_bytes(...) bytes,
@@ -619,7 +620,8 @@ nvfp4_status nvfp4_prefix_attention(const nvfp4_kv_cache* cache, const void* q, 
  * key head h / (v_heads / k_heads).  Up to 8 tokens are walked one by one (the
  * serving step: one token, the state read and written once); longer calls go by
  * chunks of 64 tokens on the matrix cores, with FP32 operands in three bf16
- * parts (24 bits), so states and gate gradients keep FP32's precision.
+ * parts (24 bits), so states and gate gradients keep FP32's precision; o, which
+ * ends in bf16, is formed of two parts (2^-16) of the states.
  *
  * A view nvfp4_rows is [batch][tokens][heads] rows of unit stride with strides
  * in elements, so column slices of a wider row of that type need no copy.  No
@@ -672,7 +674,8 @@ nvfp4_status nvfp4_gdn_forward(const nvfp4_gdn* g, const nvfp4_rows* o, float* s
  * Nothing of the forward call is needed but its inputs: the chunks' states are
  * recomputed.  d_q, d_k (summed over the value heads that share a key head, in a
  * fixed order) and d_v are bf16 rows; d_log_alpha and d_beta FP32, one value per
- * (batch, token, value head).
+ * (batch, token, value head).  The workspace holds every chunk's states: 345 KB per
+ * value head and 64 tokens (and 49 KB per key head) of 128 x 128.
  *
  * d_log_alpha is the gradient with respect to log(alpha), i.e. alpha times that
  * of alpha: what the gate's own backward pass multiplies (log alpha is

@@ -774,8 +774,8 @@ Plan plan(int heads, int dim, int64_t batch, int64_t group, int64_t prefix_len, 
     //   with 128            8 << 20: -10 to +22 (-16 to +15)
     //   with 512            6 << 20: -16 to +6 (-15 to +5);  8 << 20: -14 to +11 (-18 to +2)
     //   with 2048           6 << 20: -10 to +12 (-9 to +2);  8 << 20: -20 to +8 (-12 to +4)
-    // 64 rows: -3 to +31% (-6 to +28) at 8 and 16 << 20.  head_dim 256 has no panels (K and V of two blocks are more than the
-    // LDS holds).
+    // 64 rows: -3 to +31% (-6 to +28) at 8 and 16 << 20.  head_dim 256 has no panels: two blocks of
+    // K and V would take 134 of a compute unit's 160 KB of LDS, one workgroup of four wavefronts; not built or measured.
     q.wide = dim != 256 && rows >= kWideRows * 3 / 4 &&
              rows * heads * prefix_len >= (max_len >= 256 ? int64_t(7) << 20 : int64_t(12) << 20);
     q.prefix_tiles = (int)ceil_div(rows, q.wide ? kWideRows : 16);
