@@ -23,8 +23,8 @@
 // What bounds it: with few rows per head the cache's bytes, with many the matrix instructions and the widening
 // of the codes, which rows_panel does once for 128 rows; with little of either the latency of a range (first
 // pages, first codes, the join).  Measured, heads of 128 (a large copy moves 4.7 TB/s, a large bf16 product makes
-// 1138 TFLOP/s): 64 sequences of 64 heads on 8, a prefix of 65536 and 2048 own tokens, a scale per slot: 259 us,
-// 545 TFLOP/s in all (the prefix alone 580, with a scale per head 800; the own tokens alone 4.0 to 4.5 TB/s); 64 of
+// 1138 TFLOP/s): 64 sequences of 64 heads on 8, a prefix of 65536 and 2048 own tokens, a scale per slot: 254 us,
+// 555 TFLOP/s in all (the prefix alone 585, with a scale per head 795; the own tokens alone 3.9 to 4.3 TB/s); 64 of
 // 32 heads, 4096 and 512, a scale per head: 28 us, 5 of them the join.
 #include "mixers.h"
 
