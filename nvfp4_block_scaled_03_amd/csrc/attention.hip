@@ -487,9 +487,9 @@ __device__ __forceinline__ void rows_shared(const Params& p, int head, int base_
 
 // Many rows over a long prefix (head_dim 64 and 128): a workgroup whose wavefronts take 16 NQ rows each, all over the
 // same tokens.  The codes of 64 tokens are widened once for the four wavefronts, into LDS in the order of the
-// fragments: K [token][d] in bf16, V [d][token] (FP16, or bf16 with a scale per slot) with each 32 tokens in the order of the scores' registers and
-// the 16-byte units of a row exchanged by its number, so that neither the writes (eight rows apart) nor the reads
-// (neighbouring rows) meet on a bank.  Two blocks in LDS, one barrier per block.
+// fragments: K [token][d] in bf16, V [d][token] (FP16, or bf16 with a scale per slot) with each 32 tokens in the order of
+// the scores' registers and the 16-byte units of a row exchanged by its number, so that neither the writes (eight rows
+// apart) nor the reads (neighbouring rows) meet on a bank.  Two blocks in LDS, one barrier per block.
 constexpr int kPanel = 64;
 
 template <int D> struct Panels {
@@ -774,7 +774,7 @@ Plan plan(int heads, int dim, int64_t batch, int64_t group, int64_t prefix_len, 
     //   with 128            8 << 20: -10 to +22 (-16 to +15)
     //   with 512            6 << 20: -16 to +6 (-15 to +5);  8 << 20: -14 to +11 (-18 to +2)
     //   with 2048           6 << 20: -10 to +12 (-9 to +2);  8 << 20: -20 to +8 (-12 to +4)
-    // 64 rows: -3 to +31% (-6 to +28) at 8 and 16 << 20.  head_dim 256 has no panels: two blocks of
+    // 64 rows: 0 to +31% (-5 to +27) at 8 and 16 << 20.  head_dim 256 has no panels: two blocks of
     // K and V would take 134 of a compute unit's 160 KB of LDS, one workgroup of four wavefronts; not built or measured.
     q.wide = dim != 256 && rows >= kWideRows * 3 / 4 &&
              rows * heads * prefix_len >= (max_len >= 256 ? int64_t(7) << 20 : int64_t(12) << 20);
