@@ -661,7 +661,8 @@ typedef struct nvfp4_gdn {
 
 /* o         : bf16 rows of v_dim (written for the tokens that lens allows)
  * state_out : FP32 like state, the state after the last token; may be the same
- *             memory as g->state; NULL when not wanted
+ *             memory as g->state; NULL when not wanted.  o shares none with an
+ *             input.
  * workspace : device, >= nvfp4_gdn_forward_workspace_bytes(g), 256-byte aligned
  *             (NULL when that is 0); no initialisation; not shared by calls that
  *             may run concurrently */
@@ -681,7 +682,9 @@ nvfp4_status nvfp4_gdn_forward(const nvfp4_gdn* g, const nvfp4_rows* o, float* s
  * of alpha: what the gate's own backward pass multiplies (log alpha is
  * -exp(A) softplus(.)), and finite where alpha is 0.
  * d_state    : FP32 like state, the gradient of g->state; NULL when not wanted;
- *              may be the same memory as d_state_out */
+ *              may be the same memory as d_state_out
+ * No other output shares memory with an input: v and d_o are read again after
+ * d_v has been written. */
 size_t nvfp4_gdn_backward_workspace_bytes(const nvfp4_gdn* g);
 nvfp4_status nvfp4_gdn_backward(const nvfp4_gdn* g, const nvfp4_rows* d_o, const float* d_state_out,
                                 const nvfp4_rows* d_q, const nvfp4_rows* d_k, const nvfp4_rows* d_v,
